@@ -40,11 +40,13 @@
 // keeps the tensor cores fed.  CTAs are persistent and take tiles in turn; the
 // row tiles of one expert lie next to one another in that order, so that its
 // weights are read from L2.
+#include <atomic>
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
 #include "ep_internal.cuh"
+#include "ep_plan.h"
 
 namespace ep {
 namespace {
@@ -1354,24 +1356,44 @@ using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, voi
                               const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
                               CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
+// What is found out once is kept only once it was found: a failure is asked again.
 EncodeFn encoder() {
-  static EncodeFn fn = [] {
-    void* p = nullptr;
+  static std::atomic<void*> found;
+  void* p = found.load(std::memory_order_relaxed);
+  if (p == nullptr) {
     cudaDriverEntryPointQueryResult r;
     if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &r) != cudaSuccess ||
         r != cudaDriverEntryPointSuccess)
-      p = nullptr;
-    return reinterpret_cast<EncodeFn>(p);
-  }();
-  return fn;
+      return nullptr;
+    found.store(p, std::memory_order_relaxed);
+  }
+  return reinterpret_cast<EncodeFn>(p);
+}
+
+// A number found out once per device (0: not yet), such as a kernel's limit of
+// shared memory, which belongs to the device it was raised on.
+class PerDevice {
+  static constexpr int kDevices = 64;
+  std::atomic<int> known_[kDevices];  // zero-initialised (static storage)
+
+ public:
+  int get(int dev) const { return dev >= 0 && dev < kDevices ? known_[dev].load(std::memory_order_relaxed) : 0; }
+  void set(int dev, int v) {
+    if (dev >= 0 && dev < kDevices) known_[dev].store(v, std::memory_order_relaxed);
+  }
+};
+
+template <typename Kernel>
+cudaError_t allow_smem(Kernel kernel, size_t bytes) {
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
 }
 
 template <typename Out>
 cudaError_t launch_pair(const MatmulDev& d, const CUtensorMap& map, cudaStream_t stream) {
   auto kernel = ep_matmul_pair_kernel<Out>;
-  static const cudaError_t set = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                      static_cast<int>(PairShape::bytes(2048)));
-  if (set != cudaSuccess) return set;
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(kPairThreads);
   cfg.dynamicSmemBytes = PairShape::bytes(d.E);
@@ -1385,12 +1407,19 @@ cudaError_t launch_pair(const MatmulDev& d, const CUtensorMap& map, cudaStream_t
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  // pairs that run at once: a GPC with an odd number of SMs leaves one out
-  static const int room = [&] {
-    int n = 0;
+  // pairs that run at once, for any number of experts (a CTA has its SM to
+  // itself): a GPC with an odd number of SMs leaves one out
+  static PerDevice rooms;
+  int room = rooms.get(dev);
+  if (room == 0) {
+    err = allow_smem(kernel, PairShape::bytes(EP_MAX_EXPERTS));
+    if (err != cudaSuccess) return err;
     cfg.gridDim = dim3(static_cast<unsigned>(num_sms() / 2 * 2));
-    return cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess && n > 0 ? n : num_sms() / 2;
-  }();
+    if (cudaOccupancyMaxActiveClusters(&room, kernel, &cfg) == cudaSuccess && room > 0)
+      rooms.set(dev, room);
+    else
+      room = num_sms() / 2;
+  }
   // at most one tile per pair: the row tiles are not known here, but not more than this
   const int64_t most = (d.N + 2 * kChannels - 1) / (2 * kChannels) *
                        ((d.out_rows + kRowsPair - 1) / kRowsPair + (d.E > 1 ? d.E - 1 : 0));
@@ -1412,9 +1441,15 @@ int64_t narrow_tiles(const MatmulDev& d) {
 template <typename Out>
 cudaError_t launch_narrow(const MatmulDev& d, const CUtensorMap& map, cudaStream_t stream) {
   auto kernel = ep_matmul_narrow_kernel<Out>;
-  static const cudaError_t set = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                      static_cast<int>(NarrowShape::bytes(2048)));
-  if (set != cudaSuccess) return set;
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
+  static PerDevice allowed;
+  if (allowed.get(dev) == 0) {
+    err = allow_smem(kernel, NarrowShape::bytes(EP_MAX_EXPERTS));
+    if (err != cudaSuccess) return err;
+    allowed.set(dev, 1);
+  }
   const int64_t most = narrow_tiles(d), sms = num_sms();
   // CTAs a tile: as many as fill the SMs, each with two units of 128 k at least
   unsigned S = 1;

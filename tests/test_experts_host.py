@@ -1,0 +1,108 @@
+"""The host side of the products' launches against a stand-in for the CUDA
+runtime (fake_cudart.c), without a GPU: the library's own objects, linked with
+it, on several devices and with calls of the runtime that fail."""
+import ctypes
+import glob
+import os
+import subprocess
+
+import pytest
+
+import combine_ep_plan_gb300 as ep
+from combine_ep_plan_gb300 import build
+
+HERE = os.path.dirname(os.path.abspath(__file__))
+FAKE = 1 << 20  # device pointers: nothing reads them
+PAIR, NARROW, THIN = "matmul_pair", "matmul_narrow", "matmul_thin"
+
+
+class Launch(ctypes.Structure):
+    _fields_ = [("device", ctypes.c_int), ("grid", ctypes.c_uint), ("block", ctypes.c_uint), ("cluster", ctypes.c_uint),
+                ("smem", ctypes.c_size_t), ("overlaps", ctypes.c_int), ("name", ctypes.c_char * 256)]
+
+
+def link(out, objects):
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(build.nvcc()))), "include")
+    subprocess.run(["gcc", "-std=c11", "-Wall", "-Wextra", "-Werror", "-fPIC", "-c", os.path.join(HERE, "fake_cudart.c"),
+                    "-I", cuda, "-o", out + ".o"], check=True)
+    # -Bsymbolic: torch has brought the real runtime into the process
+    subprocess.run(["g++", "-shared", "-Wl,-z,defs", "-Wl,-Bsymbolic", "-o", out, out + ".o", *objects, "-lpthread"], check=True)
+    lib = ctypes.CDLL(out)
+    lib.fake_launch.restype = ctypes.POINTER(Launch)
+    lib.fake_fail.argtypes = [ctypes.c_char_p, ctypes.c_int, ctypes.c_int]
+    vp, i64, i32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int
+    lib.ep_matmul_int8.argtypes = [vp, vp, i64, vp, vp, i32, i64, i64, vp, vp, i32, vp, i64, vp]
+    lib.ep_matmul_status.argtypes = [vp]
+    return lib
+
+
+def built_objects():
+    build.build()
+    names = [os.path.join(build.BUILD, os.path.basename(s) + ".o") for s in build.sources()]
+    if not all(os.path.exists(n) for n in names):
+        build.build(force=True)
+    assert sorted(names) == sorted(n for n in glob.glob(os.path.join(build.BUILD, "*.o")) if n in names)
+    return names
+
+
+@pytest.fixture()
+def lib(tmp_path):
+    """A copy of its own for each test: what the library keeps starts anew."""
+    lib = link(str(tmp_path / "libep_fake.so"), built_objects())
+    lib.fake_reset()
+    return lib
+
+
+# rows of a product 512 -> 4096 with 8 experts, by the kernel that takes it
+ROWS = {PAIR: 4000, NARROW: 500, THIN: 40}
+
+
+def product(lib, rows, dtype=ep.EP_DTYPE_BF16, E=8):
+    return lib.ep_matmul_int8(FAKE, FAKE, rows, FAKE, FAKE, E, 4096, 512, FAKE, None, dtype, FAKE, rows, None)
+
+
+def launches(lib):
+    return [lib.fake_launch(i).contents for i in range(lib.fake_launches())]
+
+
+@pytest.mark.parametrize("dtype", [ep.EP_DTYPE_BF16, ep.EP_DTYPE_F32])
+@pytest.mark.parametrize("kernel", [PAIR, NARROW, THIN])
+def test_every_device_launches_every_product_kernel(lib, kernel, dtype):
+    """A kernel's limit of shared memory belongs to the device it was raised on."""
+    for device in (0, 1, 0, 3):
+        lib.fake_use_device(device)
+        assert product(lib, ROWS[kernel], dtype) == ep.EP_OK
+    got = launches(lib)
+    assert [g.device for g in got] == [0, 1, 0, 3] and all(kernel in g.name.decode() for g in got)
+    assert all(g.smem > 48 * 1024 for g in got) or kernel == THIN
+
+
+def test_pairs_fill_the_device_that_runs_them(lib):
+    """The number of pairs that run at once is asked of each device, and does not
+    depend on the first call's experts."""
+    for device, experts in ((0, 2048), (1, 8), (0, 8)):
+        lib.fake_use_device(device)
+        assert product(lib, 500000, E=experts) == ep.EP_OK
+    assert [g.grid for g in launches(lib)] == [120, 122, 120]
+
+
+@pytest.mark.parametrize("kernel", [PAIR, NARROW])
+@pytest.mark.parametrize("call", ["cudaFuncSetAttribute", "cudaGetDriverEntryPointByVersion", "cudaGetDevice",
+                                  "cudaOccupancyMaxActiveClusters"])
+def test_a_failure_is_not_kept(lib, kernel, call):
+    lib.fake_fail(call.encode(), 999, 1)
+    if call == "cudaOccupancyMaxActiveClusters" and kernel == NARROW:
+        pytest.skip("not called by this kernel")
+    first = product(lib, ROWS[kernel])
+    assert first == ep.EP_ERR_CUDA or call in ("cudaGetDevice", "cudaOccupancyMaxActiveClusters")  # a default serves
+    assert product(lib, ROWS[kernel]) == ep.EP_OK
+    last = launches(lib)[-1]
+    assert kernel in last.name.decode()
+    if kernel == PAIR:
+        assert product(lib, 500000) == ep.EP_OK and launches(lib)[-1].grid == 120
+
+
+def test_a_launch_that_is_refused_is_reported(lib):
+    lib.fake_fail(b"cudaLaunchKernelExC", 2, 1)
+    assert product(lib, ROWS[PAIR]) == ep.EP_ERR_OOM
+    assert product(lib, ROWS[PAIR]) == ep.EP_OK
