@@ -1388,6 +1388,19 @@ cudaError_t allow_smem(Kernel kernel, size_t bytes) {
   return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
 }
 
+// Clusters of n CTAs; a start before the end of the kernel ahead only where
+// the kernels wait for it.
+void set_cluster(cudaLaunchConfig_t& cfg, cudaLaunchAttribute (&attr)[2], unsigned n) {
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = n;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = EP_USE_PDL ? 2 : 1;
+}
+
 template <typename Out>
 cudaError_t launch_pair(const MatmulDev& d, const CUtensorMap& map, cudaStream_t stream) {
   auto kernel = ep_matmul_pair_kernel<Out>;
@@ -1399,14 +1412,7 @@ cudaError_t launch_pair(const MatmulDev& d, const CUtensorMap& map, cudaStream_t
   cfg.dynamicSmemBytes = PairShape::bytes(d.E);
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = 2;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
+  set_cluster(cfg, attr, 2);
   // pairs that run at once, for any number of experts (a CTA has its SM to
   // itself): a GPC with an odd number of SMs leaves one out
   static PerDevice rooms;
@@ -1460,14 +1466,7 @@ cudaError_t launch_narrow(const MatmulDev& d, const CUtensorMap& map, cudaStream
   cfg.dynamicSmemBytes = NarrowShape::bytes(d.E);
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = S;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
+  set_cluster(cfg, attr, S);
   return cudaLaunchKernelEx(&cfg, kernel, map, d);
 }
 

@@ -106,3 +106,25 @@ def test_a_launch_that_is_refused_is_reported(lib):
     lib.fake_fail(b"cudaLaunchKernelExC", 2, 1)
     assert product(lib, ROWS[PAIR]) == ep.EP_ERR_OOM
     assert product(lib, ROWS[PAIR]) == ep.EP_OK
+
+
+@pytest.mark.parametrize("kernel", [PAIR, NARROW, THIN])
+@pytest.mark.parametrize("ahead", [True, False])
+def test_launches_overlap_only_where_kernels_wait(tmp_path, kernel, ahead):
+    """Built with EP_USE_PDL=0 no kernel waits for the one ahead of it, so none
+    may start before that has ended."""
+    objects = built_objects()
+    if not ahead:
+        name = next(o for o in objects if "ep_matmul_kernels" in o)
+        plain = str(tmp_path / "plain.o")
+        ptx_only = ["-gencode", "arch=compute_103a,code=compute_103a"]  # nothing runs: no machine code
+        subprocess.run([build.nvcc(), *ptx_only, *build.NVCC_FLAGS, "-DEP_USE_PDL=0", "-c",
+                        os.path.join(build.CSRC, "ep_matmul_kernels.cu"), "-o", plain], check=True)
+        objects[objects.index(name)] = plain
+    lib = link(str(tmp_path / "libep_fake.so"), objects)
+    lib.fake_reset()
+    for rows in (ROWS[kernel], 5):
+        assert product(lib, rows) == ep.EP_OK
+    got = launches(lib)
+    assert kernel in got[0].name.decode() and [g.overlaps for g in got] == [int(ahead)] * 2
+    assert got[0].cluster == (2 if kernel == PAIR else 1)
