@@ -1,15 +1,31 @@
 // ep_ops_api.cu — the C ABI of the operators around the plan: argument checks
 // and launches.  Host code, and the status word that products without a
-// handle report to.
+// handle report to, with the kernel that takes errors out of it.
 #include <climits>
 #include <cstdint>
+#include <mutex>
 
 #include "ep_experts.h"
 #include "ep_internal.cuh"
 
 namespace {
 
-__device__ unsigned g_ops_status;
+// The errors recorded on a device, and the one that is being reported.
+__device__ unsigned g_ops_status[2];
+
+struct TakeDev {
+  unsigned* status;
+  unsigned* taken;
+};
+
+// Takes the error to report, and only it, out of the status word.  One atomic:
+// bits that products on other streams set meanwhile stay for the next report.
+__global__ void ep_take_status_kernel(TakeDev d) {
+  ep::pdl_wait();
+  const unsigned seen = *static_cast<volatile unsigned*>(d.status);
+  const unsigned report = seen & ep::kStTimeout ? ep::kStTimeout : seen & ep::kStCapacity;
+  *d.taken = report != 0 ? atomicAnd(d.status, ~report) & report : 0u;
+}
 
 constexpr unsigned long long kDefaultWaitNs = 2000000000ull;
 unsigned long long g_wait_ns = kDefaultWaitNs;
@@ -193,14 +209,14 @@ ep_status_t ep_matmul_status(ep_stream_t stream) {
   unsigned* p = ops_status();
   if (!p) return EP_ERR_CUDA;
   cudaError_t e = cudaStreamSynchronize(cu(stream));
-  unsigned st = 0;
-  if (e == cudaSuccess) e = cudaMemcpy(&st, p, sizeof st, cudaMemcpyDeviceToHost);
   if (e != cudaSuccess) return cuda_status(e);
-  if (st != 0) {
-    const unsigned zero = 0;
-    e = cudaMemcpy(p, &zero, sizeof zero, cudaMemcpyHostToDevice);
-    if (e != cudaSuccess) return cuda_status(e);
-  }
+  static std::mutex one;  // the reported word is one per device
+  const std::lock_guard<std::mutex> lock(one);
+  unsigned st = 0;
+  e = ep::launch_pdl(ep_take_status_kernel, 1, 1, cu(stream), TakeDev{p, p + 1});
+  if (e == cudaSuccess) e = cudaMemcpyAsync(&st, p + 1, sizeof st, cudaMemcpyDeviceToHost, cu(stream));
+  if (e == cudaSuccess) e = cudaStreamSynchronize(cu(stream));
+  if (e != cudaSuccess) return cuda_status(e);
   if (st & ep::kStTimeout) return EP_ERR_TIMEOUT;
   if (st & ep::kStCapacity) return EP_ERR_CAPACITY;
   return EP_OK;

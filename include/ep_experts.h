@@ -136,9 +136,10 @@ ep_status_t ep_expert_matmul_int8(ep_handle_t handle, const int8_t *a_dev, const
                                   ep_dtype_t out_dtype, void *out_dev, int64_t out_rows, ep_stream_t stream);
 
 /*
- * ep_matmul_status — synchronises `stream`, returns the first error that
+ * ep_matmul_status — synchronises `stream`, returns an error that
  * ep_matmul_int8 calls recorded on the current device (EP_OK if none) and
- * clears it.
+ * clears it, and only it: of two errors the second is returned by the next
+ * call, and one that a product on another stream records meanwhile is kept.
  */
 ep_status_t ep_matmul_status(ep_stream_t stream);
 

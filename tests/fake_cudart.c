@@ -2,8 +2,9 @@
  * A stand-in for the CUDA runtime, for tests of the library's host side without
  * a GPU: linked with the library's objects in place of the runtime, it counts
  * devices, keeps attributes by kernel and device as the runtime does, refuses
- * launches beyond them, and writes down what was launched.  No kernel runs;
- * "device memory" is host memory.
+ * launches beyond them, and writes down what was launched.  "Device memory" is
+ * host memory.  No kernel runs but one of two words, which takes the products'
+ * status and is carried out here by its definition.
  */
 #include <cuda.h>
 #include <cuda_runtime_api.h>
@@ -32,9 +33,11 @@ static struct {
 static int num_kernels;
 static struct {
   const void *symbol;
+  char name[256];
   unsigned char memory[kDevices][256];
 } symbols[32];
 static int num_symbols;
+static unsigned *late_word, late_bits;
 static char fail_name[64];
 static int fail_count, fail_code;
 
@@ -42,10 +45,19 @@ static int fail_count, fail_code;
 
 void fake_reset(void) {
   current = num_launches = fail_count = 0;
+  late_bits = 0;
   for (int i = 0; i < num_kernels; ++i)
     for (int d = 0; d < kDevices; ++d) kernels[i].smem[d] = kDefaultSmem;
 }
 void fake_use_device(int device) { current = device; }
+/* The products' status word on the current device. */
+unsigned *fake_status(void) {
+  for (int i = 0; i < num_symbols; ++i)
+    if (strstr(symbols[i].name, "g_ops_status")) return (unsigned *)symbols[i].memory[current];
+  abort();
+}
+/* `bits` come into the status right after the next copy to the host. */
+void fake_late(unsigned bits) { late_word = fake_status(), late_bits = bits; }
 /* The next `count` calls of `name` return `code`. */
 void fake_fail(const char *name, int code, int count) {
   snprintf(fail_name, sizeof fail_name, "%s", name);
@@ -86,8 +98,9 @@ void __cudaRegisterFunction(void **h, const char *host, char *device, const char
 }
 void __cudaRegisterVar(void **h, char *host, char *device, const char *name, int ext, size_t size, int constant,
                        int global) {
-  (void)h, (void)device, (void)name, (void)ext, (void)constant, (void)global;
+  (void)h, (void)device, (void)ext, (void)constant, (void)global;
   if (num_symbols == 32 || size > sizeof symbols[0].memory[0]) return;
+  snprintf(symbols[num_symbols].name, sizeof symbols[0].name, "%s", name);
   symbols[num_symbols++].symbol = host;
 }
 static int kernel_of(const void *func) {
@@ -107,9 +120,19 @@ static cudaError_t note(const void *func, unsigned grid, unsigned block, unsigne
   memcpy(l->name, kernels[k].name, sizeof l->name);
   return cudaSuccess;
 }
+/* Reports a timeout (8) before a capacity error (4), clears what is reported, leaves the rest. */
+static void take_status(void **args) {
+  struct {
+    unsigned *status, *taken;
+  } d;
+  memcpy(&d, args[0], sizeof d);
+  *d.taken = *d.status & 8 ? 8 : *d.status & 4;
+  *d.status &= ~*d.taken;
+}
 cudaError_t cudaLaunchKernelExC(const cudaLaunchConfig_t *c, const void *func, void **args) {
-  (void)args;
   MAY_FAIL("cudaLaunchKernelExC");
+  const int k = kernel_of(func);
+  if (k >= 0 && strstr(kernels[k].name, "take_status")) take_status(args);
   unsigned cluster = 1;
   int overlaps = 0;
   for (unsigned i = 0; i < c->numAttrs; ++i) {
@@ -193,6 +216,7 @@ cudaError_t cudaGetDriverEntryPointByVersion(const char *name, void **f, unsigne
   return cudaSuccess;
 }
 cudaError_t cudaGetSymbolAddress(void **at, const void *symbol) {
+  MAY_FAIL("cudaGetSymbolAddress");
   for (int i = 0; i < num_symbols; ++i)
     if (symbols[i].symbol == symbol) {
       *at = symbols[i].memory[current];
@@ -201,12 +225,13 @@ cudaError_t cudaGetSymbolAddress(void **at, const void *symbol) {
   return cudaErrorInvalidSymbol;
 }
 cudaError_t cudaMemcpy(void *to, const void *from, size_t n, enum cudaMemcpyKind kind) {
-  (void)kind;
   memcpy(to, from, n);
+  if (kind == cudaMemcpyDeviceToHost && late_bits) *late_word |= late_bits, late_bits = 0;
   return cudaSuccess;
 }
 cudaError_t cudaMemcpyAsync(void *to, const void *from, size_t n, enum cudaMemcpyKind kind, cudaStream_t s) {
   (void)s;
+  MAY_FAIL("cudaMemcpyAsync");
   return cudaMemcpy(to, from, n, kind);
 }
 cudaError_t cudaMemsetAsync(void *to, int v, size_t n, cudaStream_t s) {
@@ -243,7 +268,11 @@ cudaError_t cudaMemPoolSetAttribute(cudaMemPool_t pool, enum cudaMemPoolAttr att
   (void)pool, (void)attr, (void)v;
   return cudaSuccess;
 }
-cudaError_t cudaStreamSynchronize(cudaStream_t s) { return (void)s, cudaSuccess; }
+cudaError_t cudaStreamSynchronize(cudaStream_t s) {
+  (void)s;
+  MAY_FAIL("cudaStreamSynchronize");
+  return cudaSuccess;
+}
 cudaError_t cudaStreamCreateWithFlags(cudaStream_t *s, unsigned flags) { return (void)flags, *s = NULL, cudaSuccess; }
 cudaError_t cudaStreamDestroy(cudaStream_t s) { return (void)s, cudaSuccess; }
 cudaError_t cudaStreamWaitEvent(cudaStream_t s, cudaEvent_t e, unsigned flags) { return (void)s, (void)e, (void)flags, cudaSuccess; }

@@ -28,6 +28,7 @@ def link(out, objects):
     # -Bsymbolic: torch has brought the real runtime into the process
     subprocess.run(["g++", "-shared", "-Wl,-z,defs", "-Wl,-Bsymbolic", "-o", out, out + ".o", *objects, "-lpthread"], check=True)
     lib = ctypes.CDLL(out)
+    lib.fake_status.restype = ctypes.POINTER(ctypes.c_uint)
     lib.fake_launch.restype = ctypes.POINTER(Launch)
     lib.fake_fail.argtypes = [ctypes.c_char_p, ctypes.c_int, ctypes.c_int]
     vp, i64, i32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int
@@ -128,3 +129,36 @@ def test_launches_overlap_only_where_kernels_wait(tmp_path, kernel, ahead):
     got = launches(lib)
     assert kernel in got[0].name.decode() and [g.overlaps for g in got] == [int(ahead)] * 2
     assert got[0].cluster == (2 if kernel == PAIR else 1)
+
+
+TIMEOUT, CAPACITY = 8, 4  # bits of the status word
+
+
+def test_a_status_that_comes_in_while_another_is_read_is_kept(lib):
+    """A product on another stream may record an error between the read and the clearing."""
+    for first, late, codes in ((CAPACITY, TIMEOUT, (ep.EP_ERR_CAPACITY, ep.EP_ERR_TIMEOUT)),
+                               (TIMEOUT, CAPACITY, (ep.EP_ERR_TIMEOUT, ep.EP_ERR_CAPACITY))):
+        lib.fake_status()[0] = first
+        lib.fake_late(late)
+        assert tuple(lib.ep_matmul_status(None) for _ in codes) == codes
+        assert lib.ep_matmul_status(None) == ep.EP_OK
+
+
+def test_two_errors_are_two_reports(lib):
+    lib.fake_status()[0] = TIMEOUT | CAPACITY
+    assert [lib.ep_matmul_status(None) for _ in range(3)] == [ep.EP_ERR_TIMEOUT, ep.EP_ERR_CAPACITY, ep.EP_OK]
+
+
+def test_each_device_has_its_status(lib):
+    lib.fake_status()[0] = CAPACITY
+    lib.fake_use_device(1)
+    assert lib.ep_matmul_status(None) == ep.EP_OK
+    lib.fake_use_device(0)
+    assert lib.ep_matmul_status(None) == ep.EP_ERR_CAPACITY and lib.ep_matmul_status(None) == ep.EP_OK
+
+
+@pytest.mark.parametrize("call", ["cudaLaunchKernelExC", "cudaGetSymbolAddress", "cudaStreamSynchronize", "cudaMemcpyAsync"])
+def test_a_status_that_cannot_be_read_is_an_error(lib, call):
+    lib.fake_status()[0] = CAPACITY
+    lib.fake_fail(call.encode(), 999, 1)
+    assert lib.ep_matmul_status(None) == ep.EP_ERR_CUDA
