@@ -296,10 +296,18 @@ struct Groups {
   static size_t bytes(int E) { return 2 * sizeof(int) * (E + 1); }
 };
 
-// By one warp.  Ascending offsets make at most `most` row tiles; offsets that do
-// not ascend are held to that, so that tile indices stay within 32 bits.
+// Row tiles of nt rows that ascending offsets make at most: every group but one
+// may add a tile to those of the rows in a row, and every tile has a row.
+__host__ __device__ __forceinline__ int64_t most_row_tiles(int64_t rows, int E, int nt) {
+  const int64_t most = (rows + nt - 1) / nt + E - 1;
+  return most < rows ? most : rows;
+}
+
+// By one warp.  Offsets that do not ascend are held to as many tiles as ascending
+// ones make: tile indices stay within 32 bits, and a grid that has a cluster for
+// each tile has one for each of theirs.
 __device__ __forceinline__ void find_groups(const MatmulDev& d, const Groups& g, int NT, int lane) {
-  const int most = static_cast<int>(d.out_rows / NT) + d.E;
+  const int most = static_cast<int>(most_row_tiles(d.out_rows, d.E, NT));
   int sum = 0;
   for (int e0 = 0; e0 < d.E; e0 += 32) {
     const int e = e0 + lane;
@@ -1427,8 +1435,7 @@ cudaError_t launch_pair(const MatmulDev& d, const CUtensorMap& map, cudaStream_t
       room = num_sms() / 2;
   }
   // at most one tile per pair: the row tiles are not known here, but not more than this
-  const int64_t most = (d.N + 2 * kChannels - 1) / (2 * kChannels) *
-                       ((d.out_rows + kRowsPair - 1) / kRowsPair + (d.E > 1 ? d.E - 1 : 0));
+  const int64_t most = (d.N + 2 * kChannels - 1) / (2 * kChannels) * most_row_tiles(d.out_rows, d.E, kRowsPair);
   cfg.gridDim = dim3(static_cast<unsigned>((most < room ? most : room) * 2));
   return cudaLaunchKernelEx(&cfg, kernel, map, d);
 }
@@ -1439,9 +1446,7 @@ constexpr unsigned kMaxShare = 4;
 
 // Tiles of the few-row kernel: not more than this.
 int64_t narrow_tiles(const MatmulDev& d) {
-  int64_t row_tiles = (d.out_rows + kNarrowRows - 1) / kNarrowRows + (d.E > 1 ? d.E - 1 : 0);
-  if (row_tiles > d.out_rows) row_tiles = d.out_rows;
-  return row_tiles * ((d.N + kNarrowCh - 1) / kNarrowCh);
+  return most_row_tiles(d.out_rows, d.E, kNarrowRows) * ((d.N + kNarrowCh - 1) / kNarrowCh);
 }
 
 template <typename Out>
@@ -1476,9 +1481,7 @@ cudaError_t launch_matmul(const MatmulDev& d, bool out_bf16, cudaStream_t stream
   const bool thin = d.E == 1 ? d.out_rows <= kThinOneRows && d.out_rows * d.N * d.K <= kThinOneProducts
                              : d.out_rows <= kThinMean * static_cast<int64_t>(d.E);
   if (thin) {
-    int64_t row_tiles = (d.out_rows + kThinRows - 1) / kThinRows + (d.E > 1 ? d.E - 1 : 0);
-    if (row_tiles > d.out_rows) row_tiles = d.out_rows;
-    const unsigned grid = static_cast<unsigned>(row_tiles * ((d.N + kThinCh - 1) / kThinCh));
+    const unsigned grid = static_cast<unsigned>(most_row_tiles(d.out_rows, d.E, kThinRows) * ((d.N + kThinCh - 1) / kThinCh));
     auto kernel = d.offsets ? (out_bf16 ? ep_matmul_thin_kernel<true, __nv_bfloat16> : ep_matmul_thin_kernel<true, float>)
                             : (out_bf16 ? ep_matmul_thin_kernel<false, __nv_bfloat16> : ep_matmul_thin_kernel<false, float>);
     return launch_pdl(kernel, grid, 32 * kThinWarps, stream, d);
