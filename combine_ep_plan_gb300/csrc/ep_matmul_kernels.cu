@@ -95,20 +95,24 @@ __device__ __forceinline__ unsigned long long now_ns() {
   return t;
 }
 
+// What a CTA's copies and products in flight are waited for before it ends,
+// whatever the limit of its other waits.
+constexpr unsigned long long kDrainNs = 2000000000ull;
+
 // Every wait ends: after limit_ns it records a timeout, marks the CTA dead
 // (its other waits then give up too) and returns false.
 struct Waiter {
   unsigned* status;
   volatile int* dead;
   unsigned long long limit_ns;
-  __device__ bool slow(uint32_t bar, uint32_t parity, bool heed_dead) const {
+  __device__ bool slow(uint32_t bar, uint32_t parity, bool heed_dead, unsigned long long limit) const {
     unsigned long long t0 = 0;
     for (;;) {
       for (int i = 0; i < 64; ++i)  // the clock is slow to read
         if (mbar_try(bar, parity)) return true;
       if (heed_dead && *dead) return false;
       if (t0 == 0) t0 = now_ns();
-      if (now_ns() - t0 > limit_ns) {
+      if (now_ns() - t0 > limit) {
         atomicOr(status, kStTimeout);
         *dead = 1;
         return false;
@@ -116,7 +120,11 @@ struct Waiter {
     }
   }
   __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity) const {
-    return mbar_try(bar, parity) || slow(bar, parity, true);
+    return mbar_try(bar, parity) || slow(bar, parity, true, limit_ns);
+  }
+  // For what is in flight, also in a dead CTA.
+  __device__ __forceinline__ void drain(uint32_t bar, uint32_t parity) const {
+    if (!mbar_try(bar, parity)) slow(bar, parity, false, kDrainNs);
   }
   // By a whole warp, with one answer for it.
   __device__ __forceinline__ bool warp(uint32_t bar, uint32_t parity) const {
@@ -454,9 +462,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) ep_matmul_pair_kernel(const _
                       tile.e, w_full(s));
         }
       }
-      // loads in flight end before the CTA does
-      if (!ok)
-        for (uint32_t i = it > kW ? it - kW : 0; i < it; ++i) wait.slow(w_full(i % kW), (i / kW) & 1, false);
+      // Loads in flight end before the CTA does: those who read them may have given up.
+      for (uint32_t i = it > kW ? it - kW : 0; i < it; ++i) wait.drain(w_full(i % kW), (i / kW) & 1);
     } else if (warp == 1 && lane == 0 && rank == 0) {
       // products
       uint32_t it = 0, nt = 0;
@@ -503,10 +510,9 @@ __global__ void __launch_bounds__(kPairThreads, 1) ep_matmul_pair_kernel(const _
         mma_commit<2>(d_full);
         ++nt;
       }
-      if (!ok) {  // products in flight end before tensor memory is given back
-        mma_commit<2>(drained);
-        wait.slow(drained, 0, false);
-      }
+      // Products in flight end before tensor memory is given back: those who take them may have given up.
+      mma_commit<2>(drained);
+      wait.drain(drained, 0);
     }
   } else if (warp < 12) {
     // Weights to fp16 in tensor memory: a thread widens one channel, warps 4-7
@@ -733,6 +739,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) ep_matmul_pair_kernel(const _
   __syncwarp();
   tc_fence_before();
   __syncthreads();
+  if (rank == 1 && warp == 1 && lane == 0) wait.drain(drained, 0);  // the leader's last arrival here
+  __syncwarp();
   cluster_sync();
   tc_fence_after();
   if (warp == 1) tmem_free<2>(tmem);
@@ -898,8 +906,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
           tma_weights(at + L::kW + s * kNWBytes, &wmap, u * 128, tile.n0, tile.e, w_full(s));
         }
       }
-      if (!ok)
-        for (uint32_t i = it > kNW ? it - kNW : 0; i < it; ++i) wait.slow(w_full(i % kNW), (i / kNW) & 1, false);
+      for (uint32_t i = it > kNW ? it - kNW : 0; i < it; ++i) wait.drain(w_full(i % kNW), (i / kNW) & 1);
     } else if (warp == 1 && lane == 0) {
       uint32_t it = 0, nt = 0;
       bool ok = true;
@@ -925,10 +932,8 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
         mma_commit<1>(d_full);
         ++nt;
       }
-      if (!ok) {
-        mma_commit<1>(drained);
-        wait.slow(drained, 0, false);
-      }
+      mma_commit<1>(drained);
+      wait.drain(drained, 0);
     }
   } else if (warp < 12) {
     // Rows to fp16 in tensor memory, warps 4-7 the even stages and 8-11 the odd

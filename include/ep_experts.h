@@ -146,7 +146,8 @@ ep_status_t ep_matmul_status(ep_stream_t stream);
 /*
  * ep_debug_set_matmul_wait — test hook for the product kernels' bounded waits:
  * limit_us > 0 sets after how long a wait gives up and records EP_ERR_TIMEOUT
- * (0 restores the default, 2 s); suppress nonzero makes one CTA load no
+ * (0 restores the default, 2 s; a CTA's copies and products in flight are
+ * waited for by the default always, before it ends); suppress nonzero makes one CTA load no
  * weights, so that the waits on them run out.  Process-wide; affects calls
  * made afterwards.
  */
