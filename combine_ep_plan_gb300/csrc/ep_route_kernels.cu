@@ -11,14 +11,18 @@
 // compared at each step: 16384 x 256 grouped 27.3 us, 65536 x 128 35.0 us.)
 //
 // Selection goes by fp32 keys: the scores with their bias, or, for a softmax or
-// a sigmoid without bias and groups, the logits themselves: both rise strictly
-// with the logit, which keeps apart what the 32-bit scores would round together.
+// a sigmoid without bias, the logits themselves: both rise strictly with the
+// logit, which keeps apart what the 32-bit scores would round together.  Groups
+// are chosen by sums of scores, with or without a bias.
 // -inf marks what cannot be taken: a masked expert (logit -inf or NaN), an
 // expert of a group left out, one already taken.
 //
 // Bound by instructions, not by memory: scores that only decide the order, and
 // the softmax's sum, take the hardware's exp2 and reciprocal (together within
-// 2^-22 of the score's range); the weights themselves expf and IEEE division.
+// 2^-22 of the score's range).  The weights are expf or the sigmoid by IEEE
+// division, times the IEEE reciprocal of the sum, times the scale; where a softmax
+// is not renormalised that sum is the hardware's exp2 too (its terms' errors, 2^-22
+// each, average out over a row).
 #include <cuda_bf16.h>
 
 #include "ep_internal.cuh"
@@ -283,6 +287,16 @@ __global__ void __launch_bounds__(32 * kRouteWarps) ep_route_kernel(RouteDev d) 
         const unsigned e = at.expert(j);
         const unsigned g = per == 1 ? e : __umulhi(e, d.per_magic);
         if (!(in >> (g & 31) & 1)) key[j] = -INFINITY;
+      }
+    }
+    if (d.bias == nullptr) {  // the groups stand: their experts go by the logits, read again
+#pragma unroll
+      for (int i = 0; i < NP; ++i) {
+        float x[4];
+        load4<In>(row, at.expert(4 * i), d.E, d.vec, -INFINITY, x);
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if (key[4 * i + c] > -INFINITY) key[4 * i + c] = x[c];
       }
     }
   }

@@ -49,9 +49,10 @@ typedef enum {
  * available to the token and is left out of the softmax.  Slots without an
  * expert get index -1, the plan's unused slot, and weight 0; a token without
  * an available expert is a row of those.  A logit of +inf makes a softmax's
- * weights NaN (inf - inf).  Scores and sums are fp32; where a bias or groups
- * make the order hang on scores that differ by less than their rounding (2^-22
- * of the scores' range), either order may come out.
+ * weights NaN (inf - inf).  Scores and sums are fp32; where the order of two
+ * groups, or with a bias of two experts, hangs on scores that differ by less
+ * than their rounding (2^-22 of the scores' range), either may come out; scores
+ * that round to the same number are equal.
  *
  * logits_dev     [T,E], rows row_stride elements apart; EP_DTYPE_F32 or EP_DTYPE_BF16.
  * num_experts    E, 1..EP_MAX_EXPERTS; num_topk K, 1..min(E, EP_MAX_TOPK).

@@ -315,3 +315,35 @@ def test_route_refusals():
         ep.route_backward(z, idx.int(), w)
     with pytest.raises(TypeError):
         ep.route_backward(z, idx, w, grad_logits=torch.empty(4, 16, dtype=torch.bfloat16).cuda())
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("E,G", [(64, 8), (30, 5), (256, 8), (520, 4)])
+@pytest.mark.parametrize("T", [5, 4100])
+def test_route_groups_without_bias_go_by_the_logits(T, E, G, dtype):
+    """Inside the groups that compete, experts whose scores round to the same
+    number (a softmax far below its maximum, a saturated sigmoid) still go by
+    their logits, an expert masked by the type's lowest value last."""
+    per, lowest = E // G, torch.finfo(dtype).min
+    g = torch.Generator().manual_seed(E)
+    order = torch.randperm(2 * per, generator=g)  # of the two groups that win
+    for score, top, step in (("softmax", 0.0, -128.0), ("sigmoid", 40.0, 2.0)):
+        z = torch.full((T, E), -200.0 if score == "softmax" else -30.0)
+        place = torch.cat([torch.arange(per) + per * (G - 1), torch.arange(per) + per])
+        if score == "softmax":  # one expert at the top of each group, the others' scores underflow
+            z[:, place] = step - 0.5 * order.float()
+            z[:, place[0]], z[:, place[per]] = top, -0.5
+            z[:, place[1]] = lowest
+        else:                   # all of them round to 1
+            z[:, place] = top + step * order.float()
+        z = z.to(dtype)
+        k = min(6, 2 * per - 1)
+        idx, w = ep.route(z.cuda(), k, score, num_groups=G, topk_groups=2)
+        row = z[0].double()
+        want = sorted(place.tolist(), key=lambda e: (-float(row[e]), e))[:k]
+        assert (idx.cpu() == torch.tensor(want)).all(), score
+        assert torch.allclose(w.cpu().double(), weights64(z.double(), idx.cpu(), score, True, 1.0), rtol=RTOL, atol=1e-30)
+        # a softmax of +inf leaves nobody, as before
+        z[0, 3] = torch.inf
+        idx, _ = ep.route(z.cuda(), k, score, num_groups=G, topk_groups=2)
+        assert score == "sigmoid" or (idx[0] == -1).all()
