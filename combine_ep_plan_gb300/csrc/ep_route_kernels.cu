@@ -184,10 +184,17 @@ __device__ __forceinline__ float row_max(const float (&z)[4 * NP]) {
   return m == -INFINITY ? 0.0f : m;
 }
 
-// SCORED: the selection needs every expert's score (a bias or groups);
-// otherwise it goes by the logits.
-template <int L, int NP, bool SCORED, typename In>
+// What the selection goes by.
+enum By {
+  kLogits,       // no bias, no groups
+  kScores,       // scores and a bias, with or without groups
+  kGroupLogits,  // groups by scores, their experts by the logits (no bias).  A kernel of its own: as a
+                 // branch it cost the biased one registers, 16384 x 256 grouped 14.4 -> 18.5 us
+};
+
+template <int L, int NP, By BY, typename In>
 __global__ void __launch_bounds__(32 * kRouteWarps) ep_route_kernel(RouteDev d) {
+  constexpr bool SCORED = BY != kLogits;  // every expert's score is needed
   constexpr int V = 4 * NP;               // keys of a lane
   constexpr int kTokens = 32 / L;         // of a warp
   __shared__ float4 s_key[kRouteWarps][NP * 32];
@@ -218,7 +225,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps) ep_route_kernel(RouteDev d) 
 #pragma unroll
   for (int i = 0; i < NP; ++i) {
     float b[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (SCORED && d.bias != nullptr) load4<float>(d.bias, at.expert(4 * i), d.E, d.vec_bias, 0.0f, b);
+    if (BY == kScores) load4<float>(d.bias, at.expert(4 * i), d.E, d.vec_bias, 0.0f, b);
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
       const float x = z[4 * i + c];
@@ -289,7 +296,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps) ep_route_kernel(RouteDev d) 
         if (!(in >> (g & 31) & 1)) key[j] = -INFINITY;
       }
     }
-    if (d.bias == nullptr) {  // the groups stand: their experts go by the logits, read again
+    if (BY == kGroupLogits) {  // the groups stand: the logits are read again
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
         float x[4];
@@ -636,9 +643,9 @@ template <int L, int NP, typename In>
 cudaError_t route_lanes(const RouteDev& d, cudaStream_t stream) {
   const int tokens = kRouteWarps * (32 / L);
   const unsigned grid = static_cast<unsigned>((d.T + tokens - 1) / tokens);
-  if (d.bias != nullptr || d.G > 1)
-    return launch_pdl(ep_route_kernel<L, NP, true, In>, grid, 32 * kRouteWarps, stream, d);
-  return launch_pdl(ep_route_kernel<L, NP, false, In>, grid, 32 * kRouteWarps, stream, d);
+  if (d.bias != nullptr) return launch_pdl(ep_route_kernel<L, NP, kScores, In>, grid, 32 * kRouteWarps, stream, d);
+  if (d.G > 1) return launch_pdl(ep_route_kernel<L, NP, kGroupLogits, In>, grid, 32 * kRouteWarps, stream, d);
+  return launch_pdl(ep_route_kernel<L, NP, kLogits, In>, grid, 32 * kRouteWarps, stream, d);
 }
 
 // Few tokens do not fill the SMs eight lanes each, and end sooner a warp each:
