@@ -187,6 +187,11 @@ __device__ __forceinline__ void mma_commit(uint32_t bar) {
         : "memory");
 }
 
+// ... of a pair's products, on the barrier of this CTA alone.
+__device__ __forceinline__ void mma_commit_here(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+
 __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(addr),
@@ -511,7 +516,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) ep_matmul_pair_kernel(const _
         ++nt;
       }
       // Products in flight end before tensor memory is given back: those who take them may have given up.
-      mma_commit<2>(drained);
+      mma_commit_here(drained);
       wait.drain(drained, 0);
     }
   } else if (warp < 12) {
@@ -739,8 +744,6 @@ __global__ void __launch_bounds__(kPairThreads, 1) ep_matmul_pair_kernel(const _
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if (rank == 1 && warp == 1 && lane == 0) wait.drain(drained, 0);  // the leader's last arrival here
-  __syncwarp();
   cluster_sync();
   tc_fence_after();
   if (warp == 1) tmem_free<2>(tmem);
