@@ -33,16 +33,22 @@ class ExpertLayer:
         self.w2, self.s2 = quantize_weights(w2)
         self.topk, self.score, self.bias = topk, score, bias
         self.ranks, self.align = num_ranks, expert_alignment
-        self.handle = None
+        self.handle = self.planned = None  # the plan, and the routing it was made from
+
+    def _plan(self, idx):
+        """The handle, planned for this routing."""
+        if self.planned is not idx:
+            if self.handle is None or self.handle.T != idx.shape[0]:
+                self.handle = ep.plan(idx, self.ranks, self.w1.shape[0], self.align)
+            else:
+                self.handle.replan(idx)
+            self.planned = idx
+        return self.handle
 
     def __call__(self, x, logits):
         """x [T,H] bf16, logits [T,E] -> ([T,H] bf16, what the backward needs)."""
         idx, weights = ep.route(logits, self.topk, self.score, self.bias)
-        if self.handle is None or self.handle.T != x.shape[0]:
-            self.handle = ep.plan(idx, self.ranks, self.w1.shape[0], self.align)
-        else:
-            self.handle.replan(idx)
-        h = self.handle
+        h = self._plan(idx)
         rows = h.field("expert_offsets")[-1:]  # read on the device: no host wait
         q, qs = ep.quantize_int8(x)
         gate_up = ep.expert_matmul_int8(h, q, qs, self.w1, self.s1, gather=True)
@@ -51,9 +57,9 @@ class ExpertLayer:
         return ep.combine(h, y, weights), (logits, idx, weights, y)
 
     def router_gradient(self, saved, grad_out):
-        """The gradient of the logits."""
+        """The gradient of the logits of the call that `saved` is from, whichever calls came after it."""
         logits, idx, weights, y = saved
-        _, grad_weights = ep.combine_backward(self.handle, grad_out, y, weights)
+        _, grad_weights = ep.combine_backward(self._plan(idx), grad_out, y, weights)
         return ep.route_backward(logits, idx, grad_weights, self.score)
 
 
