@@ -827,6 +827,13 @@ def quantize_int8(x: torch.Tensor, gated: bool = False, num_rows: Optional[torch
     return codes, scales
 
 
+def _need_out(out):
+    if not isinstance(out, torch.Tensor) or out.dtype not in _FLOATS:
+        raise TypeError("out must be a bfloat16 or float32 tensor")
+    if out.dim() != 2:
+        raise ValueError("out must be a 2-d tensor")
+
+
 def _matmul_args(a, a_scale, w, w_scale, grouped, out_rows, out_dtype, out, stream):
     """-> (out, rows of a, N, K)"""
     _need(a, "a", torch.int8, 2)
@@ -850,8 +857,7 @@ def _matmul_args(a, a_scale, w, w_scale, grouped, out_rows, out_dtype, out, stre
             raise ValueError("out_dtype must be 'bf16' or 'f32'")
         out = _empty((out_rows, N), dt, a.device, stream)
     else:
-        if not isinstance(out, torch.Tensor) or out.dtype not in _FLOATS:
-            raise TypeError("out must be a bfloat16 or float32 tensor")
+        _need_out(out)
         _need(out, "out", out.dtype, 2)
         if out.shape != (out_rows, N):
             raise ValueError(f"out must be [{out_rows}, {N}]")
@@ -902,6 +908,7 @@ def expert_matmul_int8(h: EPHandle, a: torch.Tensor, a_scale: torch.Tensor, w: t
     worst case by default), else as many as `a`.  Device-side errors go to the
     handle (`h.check()`)."""
     if out is not None:
+        _need_out(out)
         out_rows = out.shape[0]
     elif gather:
         out_rows = worst_expanded_rows(h.T, h.K, h.E, h.A) if capacity is None else capacity

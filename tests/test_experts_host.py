@@ -7,6 +7,7 @@ import os
 import subprocess
 
 import pytest
+import torch
 
 import combine_ep_plan_gb300 as ep
 from combine_ep_plan_gb300 import build
@@ -162,3 +163,13 @@ def test_a_status_that_cannot_be_read_is_an_error(lib, call):
     lib.fake_status()[0] = CAPACITY
     lib.fake_fail(call.encode(), 999, 1)
     assert lib.ep_matmul_status(None) == ep.EP_ERR_CUDA
+
+
+@pytest.mark.parametrize("out,error", [([[0.0]], TypeError), ("bf16", TypeError), (torch.zeros(()), ValueError),
+                                       (torch.zeros(4, 8, dtype=torch.float16), TypeError)])
+def test_an_output_of_the_wrong_kind_is_refused_as_such(out, error):
+    class Handle:
+        T, K, E, A = 4, 1, 2, 1
+    with pytest.raises(error, match="out must be"):
+        ep.expert_matmul_int8(Handle(), torch.zeros(4, 16, dtype=torch.int8), torch.zeros(4),
+                              torch.zeros(2, 8, 16, dtype=torch.int8), torch.zeros(2, 8), out=out)
