@@ -17,11 +17,12 @@
 // Three kernels, by the mean number of rows per expert (measured at 64 experts,
 // 7168 -> 4096, each rule beside its constant):
 //   a handful   integer products straight from registers; the weights' stream
-//               is all (64 tokens top-6: 339 us, 5.5 TB/s of weights);
+//               is all (64 tokens top-6: 332 us, 5.7 TB/s of weights; in a row 308);
 //   up to 120   rows in tensor memory, weights widened in shared memory, 256
-//               channels x 128 rows a tile (1024 tokens: 403 us);
-//   more        CTA pairs, 256 channels x 256 rows (16384 tokens: 3.34 to 3.49 ms,
-//               1650 to 1727 TFLOP/s; 3.6 ms in a row, under the power limit).
+//               channels x 128 rows a tile (1024 tokens: 400 us);
+//   more        CTA pairs, 256 channels x 256 rows (16384 tokens: 3.53 ms, 1636
+//               TFLOP/s; in a row 3.6 ms, under the power limit).
+// Times here are of one launch with cold caches, unless they are called in a row.
 //
 // The pairs' kernel.  The weights are the A operand (128 channels = 128 lanes of
 // tensor memory per CTA), the rows the B operand (N columns).  Widened weights go
@@ -798,11 +799,12 @@ __global__ void __launch_bounds__(kPairThreads, 1) ep_matmul_pair_kernel(const _
 constexpr int kNarrowThreads = 768;
 constexpr int kNarrowRows = 128, kNarrowCh = 256;
 // Mean rows per expert up to which this kernel is the faster one (many experts
-// then need one row tile, some two): 64 experts, 7168 -> 4096, at 120 rows 462 us
-// against the pairs' 480, at 128 579 against 484.  One matrix: all of a tile.  And
-// wherever its tiles are so few that two CTAs or more can share each along k: one
-// matrix of 7168 -> 4096 at 256 rows 31.9 us against 52.4, at 512 42.1 against 53.4, at 768,
-// which leaves a CTA a tile, 66.7 against 53.4.
+// then need one row tile, some two): 64 experts, 7168 -> 4096, at 112 rows 460 us
+// against the pairs' 487, at 120 466 against 489, at 128 583 against 493.  (2048 ->
+// 7168 crosses earlier: at 96 rows 245 us against 276, at 120 296 against 282.)  One
+// matrix: all of a tile.  And wherever its tiles are so few that two CTAs or more
+// can share each along k: one matrix of 7168 -> 4096 at 256 rows 31.8 us against 53.4,
+// at 512 42.1 against 54.4, at 768, which leaves a CTA a tile, 66.7 against 54.4.
 constexpr int kNarrowMean = 120;
 constexpr int kNW = 3;                       // stages of weight codes, 256 channels x 128 k
 constexpr int kNS = 3;                       // widened stages, 64 k
@@ -1232,7 +1234,9 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
 // but 13.4 instead of 11.4 us for one token through one matrix.
 constexpr int kThinRows = 16, kThinCh = 16, kThinWarps = 8;
 // Mean rows per expert up to which this kernel is the faster one: 64 experts,
-// 7168 -> 4096, at 7 rows 339 us against 352, at 8 level, at 9 374 against 353.
+// 7168 -> 4096, at 6.8 rows 340 us against 351, at 7.5 348 against 351, at 8 357
+// against 352.  (K = 2048 crosses earlier: 64 experts, 2048 -> 7168, at 6 rows 217 us
+// against 204; 256 experts, 2048 -> 4096, at 6 rows 507 against 433.)
 constexpr int kThinMean = 7;
 // One matrix: up to so many rows, and products in all.  2048 -> 7168 at 32 rows
 // 17.6 us against 19.6, at 64 23.7 against 19.6; 7168 -> 4096 at 32 24.7 against 33.9;
