@@ -130,7 +130,8 @@ ep_status_t ep_matmul_int8(const int8_t *a_dev, const float *a_scales_dev, int64
  * ep_expert_matmul_int8 — ep_matmul_int8 over a plan: offsets are the handle's
  * expert_offsets; with `gather`, rows are its exp_src, so that a holds one row
  * per token and no dispatch is needed.  Device-side errors go to the handle's
- * status word (ep_sync_status).
+ * status word (ep_sync_status); as after a plan's, later plans of the handle do
+ * no work after EP_ERR_TIMEOUT until it is read there.
  */
 ep_status_t ep_expert_matmul_int8(ep_handle_t handle, const int8_t *a_dev, const float *a_scales_dev, int64_t a_rows,
                                   const int8_t *w_dev, const float *w_scales_dev, int64_t n, int64_t k, int gather,
